@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int e = vexp[2 * sl + x];
-          half_e[x] = e == kNoScale ? 0.f : static_cast<float>(e);
+          half_e[x] = e == kNoScale ? e_new : static_cast<float>(e);  // a half of zeros: any factor that keeps P finite
         }
       }
 #pragma unroll
