@@ -632,10 +632,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const int sl = i & (Lo::kScRing - 1);
           if constexpr (FMT == KVQ_FMT_INT8) {
             ksc[sl * kPxKeys + 32 * half + lane] = ksv * p.sm_scale_log2;  // the softmax's log2 factor folded in
-            if constexpr (!kFoldV) vsc[sl * kPxKeys + 32 * half + lane] = vsv;
-            // 2^e above the half's V scales (kNoScale: all zero)
+            // 2^e above the half's V scales (kNoScale: all zero), which the softmax gets as scale x 2^-e
             const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(vsv));
-            if (lane == 0) vexp[2 * sl + half] = vm ? static_cast<int>(vm >> 23) - 126 : kNoScale;
+            const int ex = vm ? static_cast<int>(vm >> 23) - 126 : kNoScale;
+            if constexpr (!kFoldV) vsc[sl * kPxKeys + 32 * half + lane] = vsv * pow2f(max(-126, min(126, -ex)));
+            if (lane == 0) vexp[2 * sl + half] = ex;
           }
           if (lane == 0) bad_pages[2 * sl + half] = cur.bad;
         }
@@ -725,12 +726,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const int kend = min(lims[rl], key_end);
     const float kconst = p.sm_scale_log2 * p.k_gs_inv;  // kfac of the non-INT8 formats
     [[maybe_unused]] const uint64_t kconst2 = pair(kconst, kconst);
-    // The row's reference is R = m + E: m its running maximum (a stale one: raised only
-    // by more than 2^8, so that O is seldom rescaled), E the exponent of the tiles' V
-    // scales (INT8; raised by more than 2^4).  With p = 2^(z - R), p x v_scale <= 2^12
-    // fits fp16 with its full precision whatever the size of V, and O and l carry the
-    // same factor 2^-E, which cancels.
-    float r_ref = -INFINITY, l_run = 0.f;  // l_run = this group's sum of 2^(z - r_ref)
+    // The row's reference is m, its running maximum (a stale one: raised only by more
+    // than 2^8, so that O is seldom rescaled): l = sum of 2^(z - m).  O (INT8) has a unit
+    // of its own besides, 2^E, E the exponent of the tiles' V scales (raised by more than
+    // 2^4), so that P' = 2^(z - m) x v_scale x 2^-E <= 2^12 fits fp16 whatever the size of
+    // V; the epilogue gives 2^E back.  Keys whose P' is below 2^-14 are off by up to 2^-25,
+    // that is 2^-24 of the range's largest |V| a key of weight 1.  INT8 rounds m up to a whole
+    // number: the differences of m and E, and the rescaling of O and l, are then exact.
+    float m_ref = -INFINITY, l_run = 0.f;  // l_run = this group's sum of 2^(z - m_ref)
     [[maybe_unused]] int e_run = kNoScale;
     auto raise_scale = [&](int sl) {
       const int e = max(vexp[2 * sl], vexp[2 * sl + 1]);
@@ -804,28 +807,24 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
         for (int t2 = 0; t2 < kPxKeys / 2; ++t2) z[t2] = pair(sv[2 * t2], sv[2 * t2 + 1]);
       }
-      const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * rs;  // log2 units
+      float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * rs;  // log2 units
+      if constexpr (FMT == KVQ_FMT_INT8) mx = ceilf(mx);
       // the row's reference after tile i - 1, from the other group; this tile's goes on
-      float r_prev = -INFINITY;
+      float m_prev = -INFINITY;
       if (i > 0) {
         if (!wait_warp(kBarM0 + 4 * ((i - 1) & 1) + w4, ((i - 1) >> 1) & 1)) {
           ok = false;
           break;
         }
-        r_prev = m_sh[((i - 1) & 1) * kPxRows + rl];
+        m_prev = m_sh[((i - 1) & 1) * kPxRows + rl];
       }
-      float e_new = 0.f, e_prev = 0.f;
-      if constexpr (FMT == KVQ_FMT_INT8) {
-        e_new = e_run == kNoScale ? 0.f : static_cast<float>(e_run);
-        e_prev = e_old == kNoScale ? 0.f : static_cast<float>(e_old);
-      }
-      float r = r_prev;
-      if (r_prev == -INFINITY || mx > r_prev - e_prev + kPxRescale) r = mx + e_new;
-      else if (e_new != e_prev) r = r_prev - e_prev + e_new;
-      m_sh[(i & 1) * kPxRows + rl] = r;
+      // how far O's unit rises (from no unit at all: O is 0)
+      const int e_up = FMT == KVQ_FMT_INT8 && e_old != kNoScale ? e_run - e_old : 0;
+      const float m = m_prev == -INFINITY || mx > m_prev + kPxRescale ? mx : m_prev;
+      m_sh[(i & 1) * kPxRows + rl] = m;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarM0 + 4 * (i & 1) + w4]);
-      const bool resc = r_prev != -INFINITY && r != r_prev;
+      const bool resc = m_prev != -INFINITY && (m != m_prev || e_up != 0);
       if (__any_sync(0xffffffffu, resc)) {
         // O is rescaled once it holds P(i-1) V(i-1), before P(i) V(i) adds to it
         if (!wait_warp(kBarO0 + ((i - 1) & 3), ((i - 1) >> 2) & 1)) {
@@ -833,7 +832,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           break;
         }
         tc_fence_after();
-        const float alpha = resc ? ex2(r_prev - r) : 1.f;
+        const float alpha = resc ? ex2(m_prev - m - static_cast<float>(e_up)) : 1.f;
 #pragma unroll 1
         for (int c = 0; c < D / 8; ++c) {
           uint32_t ov[8];
@@ -845,35 +844,39 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         tmem_st_wait();
       }
-      if (r != r_ref) {  // raised here or by the other group since this group's last tile
-        l_run *= ex2(r_ref - r);  // r_ref = -inf: 0
-        r_ref = r;
+      if (m != m_ref) {  // raised here or by the other group since this group's last tile
+        l_run *= ex2(m_ref - m);  // m_ref = -inf: 0
+        m_ref = m;
       }
       // P(i) goes over S(i), which this thread has read.  The last reader of those
       // columns before S(i), the P V product of the buffer's previous tile, was issued
       // before S(i), so the commit that reported S(i) done covered it too.
-      // pass 2: p = 2^(z - R) (a masked key's z = -inf gives exactly 0), P' = p v_scale,
-      // packed hi (+ lo)
+      // pass 2: p = 2^(z - m + d), d = (the half's exponent) - E (a masked key's z = -inf
+      // gives exactly 0), packed hi (+ lo).  The V scales that the half's tile or vs holds
+      // carry 2^-(its exponent), so p x v is P' x code in O's unit; the half's sum takes
+      // 2^-d.  A half far below the others keeps its place in the sum (d >= -60), whatever
+      // is left of it in fp16; one of zeros may take any d.
       uint64_t ps[2] = {0, 0};
-      const float nr = r == -INFINITY ? 0.f : -r;  // a row with no visible key: every z is -inf
+      const float nm = m == -INFINITY ? 0.f : -m;  // a row with no visible key: every z is -inf
       const uint64_t rs2 = pair(rs, rs);
-      uint64_t nr2 = pair(nr, nr);
-      // V folded: the V tile's halves hold V 2^-e, so P takes the factor 2^e, in the
-      // exponent, and the half's sum gives it back
-      [[maybe_unused]] float half_e[2] = {0.f, 0.f};
-      if constexpr (kFoldV) {
+      uint64_t nr2 = pair(nm, nm);
+      [[maybe_unused]] int dh[2] = {0, 0};
+      if constexpr (FMT == KVQ_FMT_INT8) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int e = vexp[2 * sl + x];
-          half_e[x] = e == kNoScale ? e_new : static_cast<float>(e);  // a half of zeros: any factor that keeps P finite
+          dh[x] = e == kNoScale ? 0 : max(-60, e - e_run);
         }
       }
 #pragma unroll
       for (int c16 = 0; c16 < kPxKeys / 16; ++c16) {  // 16 keys: 8 columns
         uint32_t ph[8], pl[8];
         [[maybe_unused]] float4 v4;  // V scales of four keys
-        if constexpr (kFoldV) {
-          if ((c16 & 1) == 0) nr2 = pair(nr + half_e[c16 >> 1], nr + half_e[c16 >> 1]);
+        if constexpr (FMT == KVQ_FMT_INT8) {
+          if ((c16 & 1) == 0) {
+            const float nd = nm + static_cast<float>(dh[c16 >> 1]);
+            nr2 = pair(nd, nd);
+          }
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -883,7 +886,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const float2 a = unpair(fma2(z[t2], rs2, nr2));
           const float2 pr = make_float2(ex2(a.x), ex2(a.y));
           uint64_t pv = pair(pr.x, pr.y);
-          ps[kFoldV ? c16 >> 1 : x & 1] = add2(ps[kFoldV ? c16 >> 1 : x & 1], pv);
+          constexpr bool kHalves = FMT == KVQ_FMT_INT8;
+          ps[kHalves ? c16 >> 1 : x & 1] = add2(ps[kHalves ? c16 >> 1 : x & 1], pv);
           if constexpr (FMT == KVQ_FMT_INT8 && !kFoldV)  // finite scales, 0 for a key that was not read
             pv = mul2(pv, (x & 1) ? pair(v4.z, v4.w) : pair(v4.x, v4.y));
           const float2 v = unpair(pv);
@@ -921,9 +925,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tmem_st8(ts + 16 * c16, ph);
         if constexpr (PLO) tmem_st8(ts + 16 * c16 + 8, pl);
       }
-      if constexpr (kFoldV) {
+      if constexpr (FMT == KVQ_FMT_INT8) {
         const float2 s0 = unpair(ps[0]), s1 = unpair(ps[1]);
-        l_run += (s0.x + s0.y) * ex2(-half_e[0]) + (s1.x + s1.y) * ex2(-half_e[1]);
+        l_run += (s0.x + s0.y) * pow2f(-dh[0]) + (s1.x + s1.y) * pow2f(-dh[1]);
       } else {
         const float2 sum = unpair(add2(ps[0], ps[1]));
         l_run += sum.x + sum.y;
@@ -935,22 +939,29 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     // ================================================================ epilogue
     // the last tile's reference is the row's; both groups bring their sums to it
-    float r_fin = r_ref;
+    float m_fin = m_ref;
     if (ok && nt > 0) {
       ok = wait_warp(kBarM0 + 4 * ((nt - 1) & 1) + w4, ((nt - 1) >> 1) & 1) &&
            wait_warp(kBarO0 + ((nt - 1) & 3), ((nt - 1) >> 2) & 1);
       tc_fence_after();
-      r_fin = m_sh[((nt - 1) & 1) * kPxRows + rl];
-      if (r_fin != r_ref) l_run *= ex2(r_ref - r_fin);
+      m_fin = m_sh[((nt - 1) & 1) * kPxRows + rl];
+      if (m_fin != m_ref) l_run *= ex2(m_ref - m_fin);
+      if constexpr (FMT == KVQ_FMT_INT8)  // O's unit after the last tile
+        if (((nt - 1) & 1) != grp) raise_scale((nt - 1) & (Lo::kScRing - 1));
     }
     l_sh[grp * kPxRows + rl] = l_run;
     soft_sync();
     ok = ok && *abort_flag == 0;  // a group that gave up leaves the row without a result
     const float l = l_sh[rl] + l_sh[kPxRows + rl];
     constexpr float kLn2 = 0.69314718055994530942f;
-    const bool any = ok && nt > 0 && r_fin != -INFINITY && l > 0.f;
-    const float inv = any ? p.v_gs_inv / l : 0.f;
-    if (grp == 0 && qoff[rl] >= 0) p.lse_part[orow_at[rl]] = any ? (r_fin + log2f(l)) * kLn2 : -INFINITY;
+    const bool any = ok && nt > 0 && m_fin != -INFINITY && l > 0.f;
+    float inv = any ? p.v_gs_inv / l : 0.f, unit = 1.f;
+    if constexpr (FMT == KVQ_FMT_INT8) {  // 2^E in two factors: E reaches beyond one's exponents
+      const int e = e_run == kNoScale ? 0 : e_run;
+      inv *= pow2f(e / 2);
+      unit = pow2f(e - e / 2);
+    }
+    if (grp == 0 && qoff[rl] >= 0) p.lse_part[orow_at[rl]] = any ? (m_fin + log2f(l)) * kLn2 : -INFINITY;
     // Each warp writes its 32 rows' half of the columns, 32 columns at a time, through a
     // patch of shared memory of its own: 128 contiguous bytes of four rows a store.
     uint8_t* patch = smem + Lo::kOAt + warp * Lo::kOPatch;
@@ -973,10 +984,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
       for (int v4 = 0; v4 < 8; ++v4) {
         float4 o;
-        o.x = any ? __uint_as_float(ov[4 * v4]) * inv : 0.f;
-        o.y = any ? __uint_as_float(ov[4 * v4 + 1]) * inv : 0.f;
-        o.z = any ? __uint_as_float(ov[4 * v4 + 2]) * inv : 0.f;
-        o.w = any ? __uint_as_float(ov[4 * v4 + 3]) * inv : 0.f;
+        o.x = any ? __uint_as_float(ov[4 * v4]) * inv * unit : 0.f;
+        o.y = any ? __uint_as_float(ov[4 * v4 + 1]) * inv * unit : 0.f;
+        o.z = any ? __uint_as_float(ov[4 * v4 + 2]) * inv * unit : 0.f;
+        o.w = any ? __uint_as_float(ov[4 * v4 + 3]) * inv * unit : 0.f;
         *reinterpret_cast<float4*>(patch + lane * Lo::kORow + 16 * v4) = o;
       }
       __syncwarp();

@@ -1,13 +1,20 @@
 """kvq_paged_prefix_attention where single values are unlike the rest: runs of V = 0, V near the ends of its range.
 
-Tolerance: as in test_gpu_prefix_range.py, the decode tests' bounds scaled with the size of V."""
+Tolerance, fp32 output: as in test_gpu_prefix_range.py, 2e-3 times the size of V.  bf16 output, INT8 cache, with w the
+softmax weights: the output's rounding, 2^-8 |out| (half a step of bf16), plus three fp16 roundings of 2^-11 a key (of
+its weight, of its V scale, of their product with the code), 3 x 2^-11 sum w |v|, plus fp16's smallest number: a factor
+below 2^-14 is off by up to 2^-25 of its unit, which is at most twice the largest V scale.  With codes up to 127 and
+max |V| = 127 x the largest scale that is 2^-24 max |V| for the V factor and its product, weighted (twice 2^-24 in all),
+and 2^-24 max |V| a key for the weight, over a sum of weights of at least 1/2: n x 2^-23 max |V|.  2e-5 sum w |v| stands
+for the logits' and the sums' fp32 arithmetic."""
 import numpy as np
 import pytest
 
+from oracle import attention as oatt
 from quantized_paged_kv_gb300 import workloads as W
 from tests import harness as H
 from tests.test_gpu_prefix import _Call, _one_group
-from tests.test_gpu_prefix_range import _check, _scale_v
+from tests.test_gpu_prefix_range import _scale_v
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +22,27 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
     H.ensure_built()
+
+
+def _check(c, size, pools=None):
+    """c's outputs against the oracle's (over its own pools, or those given)."""
+    wl = c.wl
+    pools = H.oracle_pools(wl, c.fmt, c.gs) if pools is None else pools
+    verify = lambda p: oatt.paged_verify(c.fmt, p, c.q, wl.block_tables, wl.seq_lens, wl.sm_scale)
+    ref, ref_lse = verify(pools)
+    out = c.out.float().cpu().numpy()
+    assert np.all(np.isfinite(out))
+    bound = 2e-3 * size
+    if c.out_dtype == "bf16":
+        assert c.fmt == "int8"
+        flat = dict(pools, v_codes=np.abs(pools["v_codes"].view(np.int8).astype(np.int16)).astype(np.uint8),
+                    v_scales=np.abs(pools["v_scales"]))
+        weighted, _ = verify(flat)  # sum of w |v|
+        vmax = 127 * np.nanmax(flat["v_scales"])
+        n = int(wl.seq_lens.max())
+        bound = 2.0 ** -8 * np.abs(ref) + (3 * 2.0 ** -11 + 2e-5) * weighted + (n + 1) * 2.0 ** -23 * vmax
+    assert np.all(np.abs(out - ref) <= bound), (np.abs(out - ref) / bound).max()
+    assert np.abs(c.lse.cpu().numpy() - ref_lse).max() < 1e-3
 
 
 def _peak(wl, token):
@@ -38,3 +66,31 @@ def test_runs_of_zero_v_beside_small_v(size, out_dtype, zeros, peak):
     c = _Call(wl, "int8", [0, 3], [704], splits=1, out_dtype=out_dtype, q=None if peak is None else _peak(wl, peak))
     c.launch(checked=True)
     _check(c, size)
+
+
+def _shared_only(size_of, lens=(704, 700, 690), seed=92, name="tiny_int8"):
+    """No own pages (the decode kernel's P x scale has a range of its own)."""
+    return _scale_v(_one_group(name, list(lens), max(lens), seed), size_of)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** -100, 2.0 ** -112, 2.0 ** -118, 2.0 ** 110])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ["tiny_int8", "serving_int8"])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_v_near_the_ends_of_its_range(size, out_dtype, name, splits):
+    wl = _shared_only(lambda t: size, name=name)
+    c = _Call(wl, "int8", [0, 3], [704], splits=splits, out_dtype=out_dtype)
+    c.launch(checked=True)
+    _check(c, size)
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("first,later", [(2.0 ** -112, 1.0), (1.0, 2.0 ** -112), (2.0 ** -118, 2.0 ** 110), (0.0, 2.0 ** -118),
+                                         (2.0 ** -118, 0.0)])
+@pytest.mark.parametrize("at", [16, 352, 640])
+def test_v_of_two_sizes(out_dtype, first, later, at):
+    """The small part weighs as much as the large one in the sum of weights, whatever is left of it in the result."""
+    wl = _shared_only(lambda t: first if t < at else later)
+    c = _Call(wl, "int8", [0, 3], [704], splits=1, out_dtype=out_dtype)
+    c.launch(checked=True)
+    _check(c, max(first, later))
