@@ -2,7 +2,8 @@
 // key range) and the own pages' (one a split) of every query row.
 //
 //   M = max_s lse_s,  w_s = exp(lse_s - M),  out = sum_s w_s o_s / sum_s w_s,
-//   lse = M + ln(sum_s w_s);  a partial with lse = -inf (no visible token) has weight 0.
+//   lse = M + ln(sum_s w_s);  a partial with lse = -inf (no visible token) has weight 0,
+//   one with lse = NaN (a NaN logit among the shared tokens) makes the row NaN.
 //
 // The same combination as the merge kernel's, shaped for what a prefix call leaves:
 // hundreds to thousands of rows of 10 to 40 partials (the merge kernel serves one long
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     m = mn;
   }
   if (!active) return;
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;  // NaN stays NaN
   acc.x *= inv;
   acc.y *= inv;
   acc.z *= inv;
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   } else {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at) = acc;
   }
-  if (lse_out && slice == 0 && lane == 0) lse_out[row] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+  if (lse_out && slice == 0 && lane == 0) lse_out[row] = wsum != 0.f ? m + logf(wsum) : -INFINITY;
 }
 
 }  // namespace

@@ -954,7 +954,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     ok = ok && *abort_flag == 0;  // a group that gave up leaves the row without a result
     const float l = l_sh[rl] + l_sh[kPxRows + rl];
     constexpr float kLn2 = 0.69314718055994530942f;
-    const bool any = ok && nt > 0 && m_fin != -INFINITY && l > 0.f;
+    // l = 0: no visible token (or only logits of -inf).  A NaN logit among the visible
+    // ones makes l, and so the row's partial, NaN
+    const bool any = ok && nt > 0 && l != 0.f;
     float inv = any ? p.v_gs_inv / l : 0.f, unit = 1.f;
     if constexpr (FMT == KVQ_FMT_INT8) {  // 2^E in two factors: E reaches beyond one's exponents
       const int e = e_run == kNoScale ? 0 : e_run;

@@ -9,11 +9,12 @@ and 2^-24 max |V| a key for the weight, over a sum of weights of at least 1/2: n
 for the logits' and the sums' fp32 arithmetic."""
 import numpy as np
 import pytest
+import torch
 
 from oracle import attention as oatt
 from quantized_paged_kv_gb300 import workloads as W
 from tests import harness as H
-from tests.test_gpu_prefix import _Call, _one_group
+from tests.test_gpu_prefix import _Call, _one_group, _share
 from tests.test_gpu_prefix_range import _scale_v
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +95,43 @@ def test_v_of_two_sizes(out_dtype, first, later, at):
     c = _Call(wl, "int8", [0, 3], [704], splits=1, out_dtype=out_dtype)
     c.launch(checked=True)
     _check(c, max(first, later))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "nvfp4", "bf16"])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("splits", [1, 4])
+def test_a_nan_logit_of_a_shared_token_is_not_lost(fmt, out_dtype, splits):
+    """K of one token and head is NaN: the rows that see it are NaN (not the result without the prompt); a sequence
+    that ends before it, another group and the other heads are as without it."""
+    wl = _share(W.make("tiny_int8", lens=("list", [700, 710, 290, 400, 410]), seed=93), [0, 3, 5], [640, 384])
+    gs = H.global_scales(wl, fmt)
+    c = _Call(wl, fmt, [0, 3, 5], [640, 384], splits=splits, out_dtype=out_dtype, gs=gs)
+    c.launch(checked=True)
+    out, lse = c.out.clone(), c.lse.clone()
+    kc, _, ks, _ = c.cache.views()
+    page, head, row = int(wl.block_tables[0, 300 // 16]), 1, 300 % 16
+    if fmt == "bf16":
+        kc[page, head, row].view(torch.bfloat16)[7] = float("nan")
+    elif fmt == "int8":
+        ks[page, head, row] = float("nan")
+    else:
+        ks[page, head, row, 3] = 0x7F
+    c.launch(checked=True)
+    G = wl.Hq // wl.Hkv
+    hit = torch.zeros((wl.B, 1, wl.Hq), dtype=torch.bool, device="cuda")
+    hit[:2, :, G * head:G * head + G] = True
+    assert torch.all(torch.isnan(c.out[hit])) and torch.all(torch.isnan(c.lse[hit]))
+    assert torch.equal(c.out[~hit], out[~hit]) and torch.equal(c.lse[~hit], lse[~hit])
+
+
+def test_a_nan_query_row():
+    wl = _one_group("tiny_int8", [600, 610], 592, 94)
+    q = wl.q_tokens(1)
+    q[1, 0, 5, 17] = np.nan
+    for fmt in ("int8", "bf16"):
+        c = _Call(wl, fmt, [0, 2], [592], splits=3, q=q)
+        c.launch(checked=True)
+        bad = torch.zeros((2, 1, wl.Hq), dtype=torch.bool, device="cuda")
+        bad[1, 0, 5] = True
+        assert torch.all(torch.isnan(c.out[bad])) and torch.all(torch.isnan(c.lse[bad]))
+        assert torch.all(torch.isfinite(c.out[~bad])) and torch.all(torch.isfinite(c.lse[~bad]))
