@@ -103,9 +103,14 @@ enum {
                           decode may read them (and find its first pages) while that
                           kernel is still running.  Every other input (q, the cache,
                           seq_lens) and every output is touched only after that kernel
-                          has completed.  The decode kernel is always launched as a
-                          programmatic dependent of the preceding kernel; without this
-                          flag it waits for that kernel before reading anything. */
+                          has completed.  Calls of this library overlap the end of the
+                          kernels before them, so where only such calls lie between, the
+                          kernel before those must not write them either (an append, a
+                          copy or a kernel launched in the ordinary way ends this; so does
+                          kvq_plan_splits_device for its own plan).  The decode kernel is
+                          always launched as a programmatic dependent of the preceding
+                          kernel; without this flag it waits for that kernel before
+                          reading anything. */
   KVQ_ROTATE = 8u,     /* append only: each new K and V row x is replaced by bf16(R(x)),
                           the rotation of kvq_rotate_rows, before it is quantized
                           ([capstone] "Lever one: 4-bit KV with TurboQuant": K and V

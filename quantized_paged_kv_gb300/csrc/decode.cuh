@@ -247,9 +247,6 @@ __global__ void __launch_bounds__(DecodeLayout<FMT, D>::kThreads, 1)
   constexpr int CW = Lo::kCW;
   constexpr int KS = Lo::kKSteps;
 
-  // the merge kernel is launched as a programmatic dependent: let it be scheduled
-  // (it waits for this grid's results before reading them)
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // This grid is itself launched as a programmatic dependent of the preceding
   // kernel.  Unless the caller promised that the plan and block tables are not
   // written by that kernel, wait for it before reading anything; otherwise the
@@ -260,6 +257,10 @@ __global__ void __launch_bounds__(DecodeLayout<FMT, D>::kThreads, 1)
   // write different partials; the CTA waits at its end instead, so that the merge, which
   // waits for this grid, also finds the prefix kernel's partials.
   if (p.early_start == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The merge kernel is launched as a programmatic dependent: let it be scheduled (it
+  // waits for this grid's results before reading them).  It reads the plan's split offsets
+  // without a wait, so not before the kernel that may have written them is complete.
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int HG = p.heads_per_cta;
   const int WPH = CW / HG;
   const int NST = decode_stages<FMT, D>(HG);

@@ -11,7 +11,8 @@
 // to 20 MB, written just before), so it is bound by how many loads are under way: a
 // warp takes 128 columns of a row, lane s reads partial s's lse, and 8 or 16 partials of a
 // row are in flight a warp; the slot offsets are read before the wait for the
-// kernels that write the partials.  With few rows several warps share one (a row's
+// kernels that write the partials (the prefix kernel, or a decode on its own, has waited
+// for whatever wrote them before it lets this grid start).  With few rows several warps share one (a row's
 // partials in turn) and combine through shared memory.
 // Measured as what a whole prefix call takes less (24 query heads of 256, CUDA graph,
 // against the merge kernel in its place, 10.8, 10.5 and 8.2 us of the call there): 32

@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The split offsets may be read before the preceding kernel completes when the
   // caller says so (they come from the plan, which the decode kernel never
-  // writes); the partials only after it.
+  // writes, and whose writer that kernel has waited for, unless KVQ_EARLY_START
+  // promised that there is none); the partials only after it.
   if (!offs_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float4 red_o[kMergeWarps][32];
   __shared__ float red_w[kMergeWarps];

@@ -364,9 +364,8 @@ __global__ void __launch_bounds__(kPlThreads) plan_device_kernel(const PlanParam
     }
   }
   if (flags) atomicOr(p.status, flags);
-  // The kernel that joins the partials reads the offsets before it waits for the attention
-  // kernel, which may let it start before its own wait for this one: the plan is in
-  // global memory when this block ends.
+  // A decode with KVQ_EARLY_START behind another call of this library may read the plan
+  // before this grid counts as complete: the plan is in global memory when this block ends.
   asm volatile("fence.acq_rel.gpu;" ::: "memory");
 }
 
