@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           if (is_v) {
             float vm = 0.f;
 #pragma unroll
-            for (int x = 0; x < 2 * Lo::kPasses; ++x) vm = fmaxf(vm, sc[x]);
+            for (int x = 0; x < 2 * Lo::kPasses; ++x) vm = fmaxf(vm, fabsf(sc[x]));
             const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(vm));
             const int ex = m ? static_cast<int>(m >> 23) - 126 : 0;
             const float dn = pow2f(max(-126, min(126, -ex)));
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           if constexpr (FMT == KVQ_FMT_INT8) {
             ksc[sl * kPxKeys + 32 * half + lane] = ksv * p.sm_scale_log2;  // the softmax's log2 factor folded in
             // 2^e above the half's V scales (kNoScale: all zero), which the softmax gets as scale x 2^-e
-            const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(vsv));
+            const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(vsv) & 0x7FFFFFFFu);
             const int ex = vm ? static_cast<int>(vm >> 23) - 126 : kNoScale;
             if constexpr (!kFoldV) vsc[sl * kPxKeys + 32 * half + lane] = vsv * pow2f(max(-126, min(126, -ex)));
             if (lane == 0) vexp[2 * sl + half] = ex;

@@ -135,3 +135,23 @@ def test_a_nan_query_row():
         bad[1, 0, 5] = True
         assert torch.all(torch.isnan(c.out[bad])) and torch.all(torch.isnan(c.lse[bad]))
         assert torch.all(torch.isfinite(c.out[~bad])) and torch.all(torch.isfinite(c.lse[~bad]))
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", ["one", "some", "all"])
+def test_scales_of_either_sign(out_dtype, which):
+    """The append writes scales >= 0, but a pool may hold any: code x scale is the value, as in the decode."""
+    wl = _one_group("tiny_int8", [704, 700, 690], 704, 96)
+    c = _Call(wl, "int8", [0, 3], [704], splits=2, out_dtype=out_dtype)
+    _, _, ks, vs = c.cache.views()
+    pools = H.oracle_pools(wl, "int8")
+    rng = np.random.default_rng(7)
+    sign = {"one": np.ones(ks.shape, np.float32), "some": rng.choice(np.float32([-1, 1]), ks.shape),
+            "all": np.full(ks.shape, -1, np.float32)}[which]
+    if which == "one":
+        sign[int(wl.block_tables[0, 9]), 2, 5] = -1
+    for dev, name in ((ks, "k_scales"), (vs, "v_scales")):
+        pools[name] *= sign
+        dev.mul_(torch.from_numpy(sign).cuda())
+    c.launch(checked=True)
+    _check(c, 1.0, pools)
