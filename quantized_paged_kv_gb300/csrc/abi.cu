@@ -914,6 +914,7 @@ int decode_impl(const kvq_cache* cache, const void* q, int32_t nseq, int32_t q_l
   p.num_q_heads = num_q_heads;
   p.max_pages = max_pages_per_seq;
   p.total_splits = total_splits;
+  p.item_splits = total_splits;
   p.out_bf16 = out_dtype == KVQ_OUT_BF16;
   p.early_start = (flags & KVQ_EARLY_START) ? 1 : 0;
   p.drop_copies = (flags & KVQ_TEST_STALL) ? 1 : 0;
@@ -1315,6 +1316,7 @@ int kvq_paged_prefix_attention(const kvq_cache* cache, const void* q, int32_t ba
   p.num_q_heads = num_q_heads;
   p.max_pages = max_pages_per_seq;
   p.total_splits = total_splits;
+  p.item_splits = static_cast<int32_t>(T);
   p.out_bf16 = x.out_bf16;
   p.wait_limit_ns = 2000000000ull;  // 2 s
   p.early_start = prefix->splits > 0 ? 2 : 0;  // 2: beside the prefix kernel, whose preceding kernels are done

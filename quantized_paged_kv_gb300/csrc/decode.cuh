@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(DecodeLayout<FMT, D>::kThreads, 1)
   const int4* firsts = reinterpret_cast<const int4*>(p.plan + A);
   const int32_t* roff = p.plan + A + 4 * C;
   const int4* rest = reinterpret_cast<const int4*>(p.plan + ((A + 5 * C + 1 + 3) & ~3));
-  const int n_items = p.total_splits * NHG;
+  const int n_items = p.item_splits * NHG;
   const int4 d0 = firsts[blockIdx.x];
   const int r0 = roff[blockIdx.x];
   const int r1 = roff[blockIdx.x + 1];

@@ -35,3 +35,21 @@ def test_a_plan_put_in_place_by_another_kernel(splits):
         c.launch(update=False)
         torch.cuda.synchronize()
         assert torch.equal(c.out, want[k % 2][0]) and torch.equal(c.lse, want[k % 2][1])
+
+
+def test_lists_that_run_past_the_plan_are_flagged():
+    """The last CTA's list spoiled by more than the plan holds, but less than the prefixes' partial slots: flagged, and
+    nothing behind the plan is read."""
+    from quantized_paged_kv_gb300 import KvqError
+
+    wl = _share(W.make("tiny_int8", lens=("list", [700, 340, 400]), seed=97), [0, 3], [320])
+    c = _Call(wl, "int8", [0, 3], [320], splits=40)
+    c.plan.update(c.sl)
+    good = c.plan.plan.clone()
+    C, A = c.plan.num_ctas, (wl.B + 2 + 3) // 4 * 4
+    c.plan.plan[A + 5 * C] += 3 * 40  # o[C]
+    with pytest.raises(KvqError):
+        c.launch(checked=True, update=False)
+    c.plan.plan.copy_(good)
+    c.launch(checked=True, update=False)
+    c.check()
