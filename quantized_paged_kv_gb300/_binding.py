@@ -164,6 +164,14 @@ def _here(*tensors):
             raise ValueError(f"a tensor on {t.device}, the current device is cuda:{cur}")
 
 
+def _struct_here(struct, name, cur, pinned=-1):
+    """The arrays behind a struct lie on device cur or, where that is allowed, in pinned host memory (KVCache and
+    SharedPrefix note the device, -1 for the host)."""
+    dev = getattr(struct, "device", cur)
+    if dev != cur and dev != pinned:
+        raise ValueError(f"{name} lies on {'the host' if dev < 0 else f'cuda:{dev}'}, the current device is cuda:{cur}")
+
+
 def _on(t, dtype, name, cur):
     """t is contiguous, of dtype, on device cur or in pinned host memory."""
     if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != cur:
@@ -451,6 +459,8 @@ def kvq_plan_splits_device(cache_struct, seq_lens, q_len, max_pages, prefix_stru
     cur = torch._C._cuda_getDevice()
     plan_ptr = _int32(plan, None, "plan", cur)
     _here(dev_status)
+    if prefix_struct is not None:
+        _struct_here(prefix_struct, "the prefix", cur)
     _check(lib().kvq_plan_splits_device(
         ctypes.byref(cache_struct), _int32(seq_lens, None, "seq_lens", cur), seq_lens.numel(), q_len, max_pages,
         None if prefix_struct is None else ctypes.byref(prefix_struct), total_splits, num_ctas, plan_ptr,
@@ -464,6 +474,8 @@ def kvq_paged_prefix_attention(cache_struct, q, sm_scale, block_tables, seq_lens
     odt = out.dtype
     if odt is not torch.bfloat16:
         odt = torch.float32
+    _struct_here(cache_struct, "the cache", cur, pinned=cur)
+    _struct_here(prefix_struct, "the prefix", cur)
     _on(q, torch.bfloat16, "q", cur)
     _on(out, odt, "out", cur)
     _on(workspace, torch.uint8, "workspace", cur)

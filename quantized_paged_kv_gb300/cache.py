@@ -28,6 +28,7 @@ class KVCache:
             self.k_codes.data_ptr(), self.v_codes.data_ptr(),
             self.k_scales.data_ptr() if sb else None, self.v_scales.data_ptr() if sb else None,
             num_pages, page_size, num_kv_heads, head_dim, B.FORMATS[fmt], self.k_global_scale, self.v_global_scale)
+        self.struct.device = self.k_codes.get_device()
 
     @property
     def row_bytes(self):
@@ -168,9 +169,13 @@ class SharedPrefix:
         B._need(prefix_lens, torch.int32, "prefix_lens")
         if group_offsets.numel() != prefix_lens.numel() + 1:
             raise ValueError("group_offsets must hold one value more than prefix_lens")
+        devices = {t.get_device() for t in (group_offsets, prefix_lens)} - {-1}
+        if len(devices) > 1:
+            raise ValueError("group_offsets and prefix_lens lie on different devices")
         self.group_offsets, self.prefix_lens, self.splits = group_offsets, prefix_lens, int(splits)
-        self.struct = B.KvqPrefixStruct(group_offsets.data_ptr(), prefix_lens.data_ptr(), prefix_lens.numel(),
-                                        self.splits)
+        struct = B.KvqPrefixStruct(group_offsets.data_ptr(), prefix_lens.data_ptr(), prefix_lens.numel(), self.splits)
+        struct.device = devices.pop() if devices else -1
+        self.struct = struct
 
     def __setattr__(self, name, value):
         if "struct" in self.__dict__:

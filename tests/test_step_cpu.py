@@ -271,3 +271,73 @@ def test_a_plan_with_shared_pages_is_for_prefix_decode(kvq):
             call(None, plan, q, None, None, None, 1.0)
     for ok in (NS(), NS(prefix=None), NS(prefix=NS(splits=0))):
         C._own_pages_only(ok)
+
+
+class _Fake:
+    """What the binding asks of a tensor, on any device."""
+
+    is_cuda = True
+
+    def __init__(self, dtype, shape, dev):
+        self.dtype, self.shape, self.dev = dtype, shape, dev
+        self.device = f"cuda:{dev}"
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        n = 1
+        for x in self.shape:
+            n *= x
+        return n
+
+    def data_ptr(self):
+        return P
+
+
+def test_arrays_on_another_device_are_refused(kvq, monkeypatch):
+    """Before any launch: the cache, the group arrays and every tensor of a prefix call, the group arrays of a plan."""
+    import torch
+
+    B = kvq._binding
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    f = lambda dtype, *shape, dev=0: _Fake(dtype, shape, dev)
+    i32, bf16, u8, f32 = torch.int32, torch.bfloat16, torch.uint8, torch.float32
+
+    def attend(cache_dev=0, prefix_dev=0, **over):
+        cache, prefix = _struct(kvq), _prefix(kvq)
+        cache.device, prefix.device = cache_dev, prefix_dev
+        a = dict(q=f(bf16, 4, 24, 256), bt=f(i32, 4, 20), sl=f(i32, 4), plan=f(i32, 10 ** 6), ws=f(u8, 1 << 30),
+                 out=f(f32, 4, 24, 256), lse=f(f32, 4, 24))
+        a.update(over)
+        B.kvq_paged_prefix_attention(cache, a["q"], 0.1, a["bt"], a["sl"], prefix, a["plan"], 160, 152, a["ws"], a["out"],
+                                     a["lse"], stream=type("S", (), {"cuda_stream": 0}))
+
+    def plan(prefix_dev, sl=f(i32, 4)):
+        prefix = _prefix(kvq)
+        prefix.device = prefix_dev
+        B.kvq_plan_splits_device(_struct(kvq), sl, 1, 20, prefix, 160, 152, f(i32, 10 ** 6), f(u8, 256),
+                                 stream=type("S", (), {"cuda_stream": 0}))
+
+    for over in ({"cache_dev": 1}, {"cache_dev": -1}, {"prefix_dev": 1}, {"q": f(bf16, 4, 24, 256, dev=1)},
+                 {"bt": f(i32, 4, 20, dev=1)}, {"sl": f(i32, 4, dev=1)}, {"plan": f(i32, 10 ** 6, dev=1)},
+                 {"ws": f(u8, 1 << 30, dev=1)}, {"out": f(f32, 4, 24, 256, dev=1)}, {"lse": f(f32, 4, 24, dev=1)}):
+        with pytest.raises(ValueError, match="current device"):
+            attend(**over)
+    with pytest.raises(ValueError, match="current device"):
+        plan(1)
+    with pytest.raises(ValueError, match="current device"):
+        plan(0, f(i32, 4, dev=1))
+
+
+def test_a_prefix_knows_its_device(kvq, monkeypatch):
+    import torch
+
+    f = lambda dev, n: _Fake(torch.int32, (n,), dev)
+    assert kvq.SharedPrefix(f(1, 3), f(1, 2), 2).struct.device == 1
+    with pytest.raises(ValueError, match="different devices"):
+        kvq.SharedPrefix(f(0, 3), f(1, 2), 2)
+    assert kvq.KVCache("int8", 4, 1, 128, device="meta").struct.device == -1
