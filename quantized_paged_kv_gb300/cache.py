@@ -175,6 +175,9 @@ class SharedPrefix:
         self.group_offsets, self.prefix_lens, self.splits = group_offsets, prefix_lens, int(splits)
         struct = B.KvqPrefixStruct(group_offsets.data_ptr(), prefix_lens.data_ptr(), prefix_lens.numel(), self.splits)
         struct.device = devices.pop() if devices else -1
+        # what a plan depends on (nothing of the groups where no page is shared)
+        self.key = ((group_offsets.data_ptr(), prefix_lens.data_ptr(), prefix_lens.numel(), self.splits) if self.splits
+                    else None)
         self.struct = struct
 
     def __setattr__(self, name, value):
@@ -224,8 +227,9 @@ class DevicePlan:
 def prefix_decode(cache, plan, prefix, q, block_tables, seq_lens, out, sm_scale, lse_out=None, checked=False,
                   stream=None):
     """Attention of a batch whose sequences share prefixes: q [B, Hq, D], or [B, q_len, Hq, D] (causal, as verify);
-    plan: DevicePlan(..., prefix=prefix), updated with these lengths."""
-    if plan.prefix is None or plan.prefix.splits != prefix.splits:
+    plan: DevicePlan(..., prefix=prefix), updated with these lengths; prefix: the plan's, or another one over the same
+    tensors."""
+    if plan.prefix is not prefix and (plan.prefix is None or plan.prefix.key != prefix.key):
         raise ValueError("the plan was made without this prefix")
     T = q.shape[1] if q.dim() == 4 else 1
     if plan.q_len != T or plan.num_seqs != q.shape[0]:

@@ -341,3 +341,35 @@ def test_a_prefix_knows_its_device(kvq, monkeypatch):
     with pytest.raises(ValueError, match="different devices"):
         kvq.SharedPrefix(f(0, 3), f(1, 2), 2)
     assert kvq.KVCache("int8", 4, 1, 128, device="meta").struct.device == -1
+
+
+def test_a_plan_is_for_its_own_prefix(kvq, monkeypatch):
+    """prefix_decode takes the prefix that the plan was made with, or one over the same tensors: another one with the
+    same number of splits would be read with offsets that the plan does not have."""
+    from types import SimpleNamespace as NS
+
+    import torch
+
+    from quantized_paged_kv_gb300 import cache as C
+
+    calls = []
+    monkeypatch.setattr(kvq._binding, "kvq_paged_prefix_attention", lambda *a: calls.append(a))
+
+    def prefix(offs, lens, splits=2):
+        a, b = _Fake(torch.int32, (3,), 0), _Fake(torch.int32, (2,), 0)
+        a.data_ptr, b.data_ptr = lambda: offs, lambda: lens
+        return kvq.SharedPrefix(a, b, splits)
+
+    q, bt = torch.zeros(4, 8, 128), torch.zeros(4, 20)
+    made = prefix(P, P + 64)
+    plan = NS(prefix=made, q_len=1, num_seqs=4, max_pages=20, plan=None, total_splits=0, num_ctas=0, workspace=None)
+    call = lambda p: C.prefix_decode(NS(struct=None), plan, p, q, bt, None, None, 1.0)
+    for ok in (made, prefix(P, P + 64)):
+        call(ok)
+    assert len(calls) == 2
+    for other in (prefix(P + 256, P + 64), prefix(P, P + 128), prefix(P, P + 64, 3), prefix(P, P + 64, 0)):
+        with pytest.raises(ValueError, match="without this prefix"):
+            call(other)
+    plan.prefix = prefix(P, P + 64, 0)  # nothing shared: the groups are not read
+    call(prefix(P + 256, P + 512, 0))
+    assert len(calls) == 3
