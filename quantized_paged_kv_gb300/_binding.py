@@ -156,6 +156,11 @@ def _need(t, dtype, name, device=True):
         raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
 
 
+def _device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be device memory")
+
+
 def _here(*tensors):
     """The tensors of one call lie on the current device (pinned host memory aside)."""
     cur = torch._C._cuda_getDevice()
@@ -411,6 +416,7 @@ def tables_buffers(block_tables, slot_mapping, seq_lens, query_start, page_start
     _need(block_tables, torch.int32, "block_tables")
     _need(slot_mapping, torch.int64, "slot_mapping")
     _need(workspace, torch.uint8, "workspace")
+    _device(workspace, "workspace")
     for t, m, name in ((seq_lens, n, "seq_lens"), (query_start, n + 1, "query_start"), (page_start, n + 1, "page_start"),
                        (free_head_out, 1, "free_head_out")):
         _int32(t, m, name, dev)
@@ -458,6 +464,8 @@ def kvq_plan_splits_device(cache_struct, seq_lens, q_len, max_pages, prefix_stru
     """prefix_struct: a KvqPrefixStruct or None; plan: int32 on the device; dev_status: any device word."""
     cur = torch._C._cuda_getDevice()
     plan_ptr = _int32(plan, None, "plan", cur)
+    _device(plan, "plan")
+    _device(dev_status, "dev_status")
     _here(dev_status)
     if prefix_struct is not None:
         _struct_here(prefix_struct, "the prefix", cur)
@@ -479,6 +487,7 @@ def kvq_paged_prefix_attention(cache_struct, q, sm_scale, block_tables, seq_lens
     _on(q, torch.bfloat16, "q", cur)
     _on(out, odt, "out", cur)
     _on(workspace, torch.uint8, "workspace", cur)
+    _device(workspace, "workspace")
     if lse_out is not None:
         _on(lse_out, torch.float32, "lse_out", cur)
     bt, sl, pl = (_int32(block_tables, None, "block_tables", cur), _int32(seq_lens, None, "seq_lens", cur),

@@ -276,11 +276,15 @@ def test_a_plan_with_shared_pages_is_for_prefix_decode(kvq):
 class _Fake:
     """What the binding asks of a tensor, on any device."""
 
-    is_cuda = True
-
-    def __init__(self, dtype, shape, dev):
-        self.dtype, self.shape, self.dev = dtype, shape, dev
+    def __init__(self, dtype, shape, dev):  # dev -1: pinned host memory
+        self.dtype, self.shape, self.dev, self.is_cuda = dtype, shape, dev, dev >= 0
         self.device = f"cuda:{dev}"
+
+    def is_pinned(self):
+        return self.dev < 0
+
+    def dim(self):
+        return len(self.shape)
 
     def get_device(self):
         return self.dev
@@ -373,3 +377,24 @@ def test_a_plan_is_for_its_own_prefix(kvq, monkeypatch):
     plan.prefix = prefix(P, P + 64, 0)  # nothing shared: the groups are not read
     call(prefix(P + 256, P + 512, 0))
     assert len(calls) == 3
+
+
+def test_workspaces_and_plans_are_device_memory(kvq, monkeypatch):
+    """Pinned host memory serves q, tables and lengths; what the kernels count and exchange partials in is the device's."""
+    import torch
+
+    B = kvq._binding
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    f = lambda dtype, *shape, dev=0: _Fake(dtype, shape, dev)
+    i32, bf16, u8, f32 = torch.int32, torch.bfloat16, torch.uint8, torch.float32
+    stream = type("S", (), {"cuda_stream": 0})
+    with pytest.raises(ValueError, match="workspace must be device memory"):
+        B.kvq_paged_prefix_attention(_struct(kvq), f(bf16, 4, 24, 256), 0.1, f(i32, 4, 20), f(i32, 4), _prefix(kvq),
+                                     f(i32, 10 ** 6), 160, 152, f(u8, 1 << 30, dev=-1), f(f32, 4, 24, 256), stream=stream)
+    for plan, status, name in ((f(i32, 10 ** 6, dev=-1), f(u8, 256), "plan"), (f(i32, 10 ** 6), f(u8, 256, dev=-1), "dev_status"),
+                               (f(i32, 10 ** 6), torch.zeros(256, dtype=u8), "dev_status")):
+        with pytest.raises(ValueError, match=name + " must be device memory"):
+            B.kvq_plan_splits_device(_struct(kvq), f(i32, 4), 1, 20, None, 160, 152, plan, status, stream=stream)
+    with pytest.raises(ValueError, match="workspace must be device memory"):
+        B.tables_buffers(f(i32, 4, 10), f(torch.int64, 64), f(i32, 4), f(i32, 5), f(i32, 5), f(i32, 1), f(u8, 256, dev=-1))
+    assert B.tables_buffers(f(i32, 4, 10), f(torch.int64, 64), f(i32, 4), f(i32, 5), f(i32, 5), f(i32, 1), f(u8, 256))[0] == 4
