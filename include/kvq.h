@@ -492,7 +492,8 @@ typedef struct kvq_prefix {
   const int32_t* prefix_lens;   /* device int32 [num_groups], tokens */
   int32_t num_groups;           /* 1 .. batch */
   int32_t splits;               /* 1 .. 64 key ranges of a prefix (kvq_prefix_splits); 0: nothing is
-                                 * shared, every page is a sequence's own and the arrays are not read */
+                                 * shared, every page is a sequence's own, and the other fields are not
+                                 * read (the arrays may be NULL) */
 } kvq_prefix;
 
 /* A default for kvq_prefix.splits: the S that minimises a model of the prefix

@@ -233,6 +233,7 @@ int allow_smem(const void* kernel, int bytes, int slot) {
 enum { kSmemPlan = 0, kSmemTables = 1, kSmemPrefix = 4 };  // slots of allow_smem; the prefix kernels take 12
 
 int check_prefix(const kvq_prefix* p, int32_t batch) {
+  if (p->splits == 0) return KVQ_OK;  // nothing is shared: the rest is not read
   if (!p->group_offsets || !p->prefix_lens) return fail(KVQ_ERR_INVALID_ARG, "prefix arrays are NULL");
   if (p->num_groups < 1 || p->num_groups > batch)
     return fail(KVQ_ERR_INVALID_ARG, "num_groups %d not in [1, batch %d]", p->num_groups, batch);
@@ -1265,7 +1266,9 @@ int kvq_paged_prefix_attention(const kvq_cache* cache, const void* q, int32_t ba
   }
   // row blocks: rows / 128 rounded up in every group
   const int64_t rows = V * G;
-  const int64_t blocks = prefix->num_groups == 1 ? (rows + inst.rows - 1) / inst.rows : rows / inst.rows + prefix->num_groups;
+  const int64_t blocks = prefix->splits == 0       ? 0
+                         : prefix->num_groups == 1 ? (rows + inst.rows - 1) / inst.rows
+                                                   : rows / inst.rows + prefix->num_groups;
   if (blocks > 65535 || cache->num_kv_heads > 65535 || (int64_t)total_splits * num_q_heads > 0x7FFFFFFF)
     return fail(KVQ_ERR_UNSUPPORTED, "grid too large");
   for (int i = 0; i < 2; ++i) {

@@ -53,3 +53,27 @@ def test_lists_that_run_past_the_plan_are_flagged():
     c.plan.plan.copy_(good)
     c.launch(checked=True, update=False)
     c.check()
+
+
+def test_nothing_shared_without_groups():
+    """An empty kvq_prefix with splits = 0: the plan without a prefix, and the decode's result."""
+    from quantized_paged_kv_gb300 import DevicePlan, _binding as B, decode
+
+    wl = W.make("tiny_int8", lens=("list", [700, 40, 0, 16]), seed=98)
+    cache = H.gpu_cache(wl, "int8")
+    sl, bt = torch.from_numpy(wl.seq_lens).cuda(), torch.from_numpy(wl.block_tables).cuda()
+    q = torch.from_numpy(wl.q()).to(torch.bfloat16).cuda()
+    plan = DevicePlan(cache, wl.B, wl.Hq, bt.shape[1])
+    plan.update(sl, checked=True)
+    want, out = torch.empty(wl.B, wl.Hq, wl.D, device="cuda"), torch.empty(wl.B, wl.Hq, wl.D, device="cuda")
+    lse = torch.empty(wl.B, wl.Hq, device="cuda")
+    decode(cache, plan, q, bt, sl, want, wl.sm_scale, checked=True)
+    empty = B.KvqPrefixStruct(None, None, 0, 0)
+    again = plan.plan.clone().fill_(-9)
+    B.kvq_plan_splits_device(cache.struct, sl, 1, bt.shape[1], empty, plan.total_splits, plan.num_ctas, again,
+                             plan.workspace, B.KVQ_CHECKED)
+    assert torch.equal(again, plan.plan)
+    B.kvq_paged_prefix_attention(cache.struct, q, wl.sm_scale, bt, sl, empty, again, plan.total_splits, plan.num_ctas,
+                                 plan.workspace, out, lse, B.KVQ_CHECKED)
+    assert (out - want).abs().max() <= 4e-3  # each within 2e-3 of the oracle
+    assert torch.equal(torch.isneginf(lse), (sl == 0)[:, None].expand_as(lse))

@@ -398,3 +398,12 @@ def test_workspaces_and_plans_are_device_memory(kvq, monkeypatch):
     with pytest.raises(ValueError, match="workspace must be device memory"):
         B.tables_buffers(f(i32, 4, 10), f(torch.int64, 64), f(i32, 4), f(i32, 5), f(i32, 5), f(i32, 1), f(u8, 256, dev=-1))
     assert B.tables_buffers(f(i32, 4, 10), f(torch.int64, 64), f(i32, 4), f(i32, 5), f(i32, 5), f(i32, 1), f(u8, 256))[0] == 4
+
+
+def test_nothing_shared_needs_no_groups(kvq):
+    """splits = 0: NULL arrays and any group count pass the checks of both calls, up to those of the buffers' sizes
+    (3), which come after."""
+    for p in (_prefix(kvq, None, None, 0, 0), _prefix(kvq, None, None, 10 ** 9, 0), _prefix(kvq, P, P, -3, 0)):
+        assert _plan(kvq, prefix=p, total=152, cap=100) == 3
+        assert _attend(kvq, prefix=p, total=152, ws_bytes=4096) == 3
+    assert _plan(kvq, prefix=_prefix(kvq, None, None, 0, -1)) == 1
