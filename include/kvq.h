@@ -496,9 +496,11 @@ typedef struct kvq_prefix {
                                  * read (the arrays may be NULL) */
 } kvq_prefix;
 
-/* A default for kvq_prefix.splits: the S that minimises a model of the prefix
- * kernel's time fitted to measured calls (see kvq_prefill_splits), for prefix_len
- * shared tokens (the longest group's) and num_groups groups; 0 where the sequences
+/* A default for kvq_prefix.splits: the S that minimises the model of
+ * kvq_prefill_splits, which was fitted to prefill calls (the prefix kernel's tiles
+ * take about 1.1 us instead of its 1.9), for prefix_len shared tokens (the longest
+ * group's) and num_groups groups, among those whose key ranges hold at most 4,096 tokens
+ * (64 where that takes more: past 262,144 shared tokens); 0 where the sequences
  * are expected to read the shared pages faster each for itself (few sequences or a
  * short prefix: under about 45,000 shared tokens x sequences at 4 KV heads of 256).
  * >= 0, or minus a kvq_status.  target_ctas: the SM count (0: the current device's). */

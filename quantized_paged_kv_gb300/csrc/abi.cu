@@ -269,18 +269,20 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // measured prefill calls at 32K keys (2,048 / 512 / 6 tokens, S = 1 .. 64):
 //   waves(S) x (10 us + 1.9 us x tiles a split) + [S > 1] (3.5 us + partials)
 // with waves(S) = ceil(items x S / CTAs a wave), one CTA an SM, and the merge's
-// partials written and read once at 6 TB/s.  Ties go to the smaller S.
+// partials written and read once at 6 TB/s.  Ties go to the smaller S.  `least`: the
+// smallest S wanted.
 int64_t pick_key_splits(int64_t items, int64_t pages, int64_t partial_bytes_per_split, int64_t ctas,
-                        double* model_us = nullptr) {
+                        double* model_us = nullptr, int64_t least = 1) {
   const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(64, pages / 4));
-  int64_t best = 1;
+  const int64_t from = std::min(std::max<int64_t>(least, 1), cap);
+  int64_t best = from;
   double best_us = 0.0;
-  for (int64_t S = 1; S <= cap; ++S) {
+  for (int64_t S = from; S <= cap; ++S) {
     const int64_t waves = (items * S + ctas - 1) / ctas;
     const int64_t tiles = (pages + 4 * S - 1) / (4 * S);
     double us = (double)waves * (10.0 + 1.9 * (double)tiles);
     if (S > 1) us += 3.5 + 2.0 * (double)partial_bytes_per_split * (double)S / 6.0e6;
-    if (S == 1 || us < best_us) {
+    if (S == from || us < best_us) {
       best = S;
       best_us = us;
     }
@@ -1111,7 +1113,13 @@ int32_t kvq_prefix_splits(const kvq_cache* cache, int32_t batch, int32_t q_len, 
   const int64_t V = (int64_t)batch * q_len, pages = prefix_len / cache->page_size;
   const int64_t items = (V * G / num_groups + inst.rows - 1) / inst.rows * num_groups * cache->num_kv_heads;
   const int64_t part = V * num_q_heads * cache->head_dim * 4;  // bytes of partials a split
-  const int64_t S = pick_key_splits(items, pages, part, sms);
+  // Key ranges of at most 4,096 tokens (256 pages), as far as 64 of them reach: the tensor
+  // cores' accumulator truncates, and fp32 output is off by 0.9e-5 of its size at 4,096
+  // tokens a range, by 1.9e-5 at 8,192.  Whole waves of the shorter ranges cost little where
+  // they are not those that the model takes anyway (prefixes past 40K tokens; us, longer /
+  // shorter ranges: INT8, 4 heads of 256, 32 sequences on 100K tokens 153 / 158, on 128K 193 / 192;
+  // 8 heads of 128, 64 sequences of 2 tokens on 64K 234 / 250; NVFP4, 48 sequences on 128K 247 / 287).
+  const int64_t S = pick_key_splits(items, pages, part, sms, nullptr, (pages + 255) / 256);
   // Does sharing pay?  What the prefix kernel and its partials add to a call against what
   // the decode kernel takes for the shared pages once a sequence (through L2), or the
   // verify call's tensor-core route for them; fitted at 1 .. 64 sequences and 1 or 4 query

@@ -407,3 +407,16 @@ def test_nothing_shared_needs_no_groups(kvq):
         assert _plan(kvq, prefix=p, total=152, cap=100) == 3
         assert _attend(kvq, prefix=p, total=152, ws_bytes=4096) == 3
     assert _plan(kvq, prefix=_prefix(kvq, None, None, 0, -1)) == 1
+
+
+def test_default_key_ranges_stay_short_enough_for_fp32(kvq):
+    """The accumulator's truncation grows with a range's tokens: the default takes at most 4,096, as far as 64 ranges
+    reach."""
+    f = kvq.kvq_prefix_splits
+    for fmt, hkv, hq, d in (("int8", 4, 24, 256), ("int8", 8, 32, 128), ("nvfp4", 2, 16, 256), ("bf16", 4, 28, 128)):
+        s = _struct(kvq, fmt, hkv=hkv, d=d)
+        for B, q in ((16, 1), (48, 1), (64, 6), (200, 4)):
+            for n in (4096, 5000, 8192, 20000, 77777, 131072, 262144):
+                S = f(s, B, q, hq, 1, n, 152)
+                assert S == 0 or -(-n // 16) <= 256 * S, (fmt, B, q, n, S)
+            assert f(s, B, q, hq, 1, 300000, 152) == 64
