@@ -576,7 +576,8 @@ int kvq_plan_splits_device(const kvq_cache* cache, const int32_t* seq_lens, int3
  * own tokens it empties its split, as in the decode.)
  * INT8, NVFP4 and BF16 caches at head_dim 128 or 256; 1 <=
  * num_q_heads / num_kv_heads <= 8.  INT8_G32 is refused, as by the prefill.  q and
- * out are device memory.  INT8: the shared pages take V of any finite size; the own
+ * out are device memory.  INT8: the shared pages take V of any finite size, each key off by
+ * up to 2^-22 of the largest |V| in its key range besides the relative roundings; the own
  * pages take what the decode takes (its P x V scale is an fp16 pair: scales below 65504,
  * and an absolute error of up to 127 x 2^-25 a key for V far below 1).
  */

@@ -200,9 +200,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   constexpr bool kBf16 = T::kBf16Mma;
   constexpr int KS = D / 16;  // k-steps of S
   // INT8 with bf16 output: V's scales go into the V tile, fp16(code x scale 2^-e) (two
-  // roundings of 2^-12, below the output's own 2^-9), which spares the softmax a
-  // multiplication and a shared-memory read a key; with fp32 output the tile holds the
-  // exact codes and the scales are folded into P.
+  // roundings of 2^-11, an eighth of the output's own 2^-8; P has one more), which spares the
+  // softmax a multiplication and a shared-memory read a key.  2^e is the unit of 32 keys: a
+  // scale below 2^-14 of their largest is subnormal in fp16, its key's V off by up to 2^-24 of
+  // the largest |V| among them, as P' is with the scales folded into it (see the softmax).
+  // With fp32 output the tile holds the exact codes and the scales are folded into P.
+  // BF16 cache with bf16 output: P is one bf16 term, as in the decode kernel: up to 2^-8 a
+  // weight, like the output's own rounding (rms error 2.2e-3 in all where the output's
+  // rounding alone makes 1.7e-3).
   constexpr bool kFoldV = FMT == KVQ_FMT_INT8 && !PLO;
   constexpr uint32_t kIdescS = umma_idesc_f16(kPxRows, kPxKeys, kBf16, false);
   constexpr uint32_t kIdescPV = umma_idesc_f16(kPxRows, D, kBf16, true);

@@ -39,3 +39,41 @@ def test_fp32_output_by_tokens_of_a_range(fmt, name, n, splits):
     assert np.linalg.norm(d) <= bound * np.linalg.norm(ref[rows]), np.linalg.norm(d) / np.linalg.norm(ref[rows])
     # lse: logits and sums in fp32, of size up to 2^5
     assert np.abs(c.lse.cpu().numpy()[rows] - ref_lse[rows]).max() <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 2.0 ** -14, 2.0 ** -18])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+def test_int8_v_of_two_sizes_in_every_tile(ratio, out_dtype):
+    """V alternates between sizes 1 and `ratio` from token to token; one query of each row of heads weighs a small token
+    most, one a large token.  Beside the relative terms (bf16: 2^-8 of the output, three fp16 roundings of 2^-11 a key;
+    fp32: the accumulator's n / 8 x 2^-23 and 2^-20) a key's factor is off by fp16's smallest number, 2^-25 of a unit of
+    at most twice the largest scale: w x 2^-23 max |V| for V's factor and product, and for the weight, whose sum is at
+    least 1/2, 2^-23 max |V|, or all of the key where that is less."""
+    n = 704
+    wl = _one_group("tiny_int8", [n, n, n], n, 102)
+    plain = wl.kv
+    wl.kv = lambda b: (plain(b)[0], W.bf16_round(plain(b)[1] * np.where(np.arange(n) % 2, ratio, 1.0)[:, None, None]))
+    q = wl.q_tokens(1)
+    G = wl.Hq // wl.Hkv
+    for b, token in ((0, 301), (1, 300)):
+        q[b, 0] += np.repeat(plain(2)[0][token], G, 0).reshape(wl.Hq, wl.D)
+    q = W.bf16_round(q)
+    c = _Call(wl, "int8", [0, 3], [n], splits=1, out_dtype=out_dtype, q=q)
+    c.launch(checked=True)
+    out = c.out.float().cpu().numpy()[:, 0].astype(np.float64)
+    pools = H.oracle_pools(wl, "int8")
+    for b in range(3):
+        slots = wl.slots(b)
+        for h in range(wl.Hkv):
+            k = oatt.cache_rows("int8", pools["k_codes"], pools["k_scales"], slots, h)
+            v = oatt.cache_rows("int8", pools["v_codes"], pools["v_scales"], slots, h)
+            z = np.asarray(q[b, 0, G * h:G * h + G], np.float64) @ k.T * wl.sm_scale
+            w = np.exp(z - z.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            ref, size, vmax = w @ v, w @ np.abs(v), np.abs(v).max()
+            rel = 2.0 ** -8 * np.abs(ref) + 3 * 2.0 ** -11 * size if out_dtype == "bf16" else \
+                (n / 8 * 2.0 ** -23 + 2.0 ** -20) * size
+            lost = np.stack([np.minimum(2.0 ** -23 * vmax, 2 * w[g][:, None] * np.abs(v)).sum(0) for g in range(G)])
+            bound = rel + 2e-5 * size + 2.0 ** -23 * vmax + lost
+            d = np.abs(out[b, G * h:G * h + G] - ref)
+            assert np.all(d <= bound), (d / bound).max()
