@@ -570,10 +570,11 @@ int kvq_plan_splits_device(const kvq_cache* cache, const int32_t* seq_lens, int3
  * too few partial slots it sets KVQ_DEV_BAD_PLAN.
  * The tensor cores' accumulator truncates: with fp32 output the error relative to the
  * output's size grows with the tokens of a key range (1e-5 at 4,096; see splits).
- * Tokens that no row of a group sees are never read; a NaN or an infinity stored in V of
- * a shared token that one row sees may reach rows of its group that end before it.  A
- * NaN logit of a shared token makes the rows that see it, and their lse, NaN.  (Among the
- * own tokens it empties its split, as in the decode.)
+ * Tokens that no row of a group sees are never read, and a NaN or an infinity stored in a
+ * shared token reaches no row that ends before it (the rows of its key range that do are
+ * then made again key by key, which is slow).  A NaN logit of a shared token makes the
+ * rows that see it, and their lse, NaN.  (Among the own tokens it empties its split, as in
+ * the decode.)
  * INT8, NVFP4 and BF16 caches at head_dim 128 or 256; 1 <=
  * num_q_heads / num_kv_heads <= 8.  INT8_G32 is refused, as by the prefill.  q and
  * out are device memory.  INT8: the shared pages take V of any finite size, each key off by

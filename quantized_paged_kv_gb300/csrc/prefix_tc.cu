@@ -190,6 +190,56 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Element d of a pool row.
+template <int FMT, int D>
+__device__ __forceinline__ float pool_value(const uint8_t* codes, const uint8_t* scales, int64_t row, int d) {
+  if constexpr (FMT == KVQ_FMT_BF16) {
+    return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(codes)[row * D + d] << 16);
+  } else if constexpr (FMT == KVQ_FMT_INT8) {
+    return static_cast<float>(reinterpret_cast<const int8_t*>(codes)[row * D + d]) *
+           reinterpret_cast<const float*>(scales)[row];
+  } else {
+    const uint32_t n = codes[row * (D / 2) + d / 2] >> (4 * (d & 1));
+    const uint32_t two = n & 6u;  // E2M1: 0, 0.5, then (1 + half the low bit) x 2^((n & 6) / 2 - 1)
+    const float mag = two ? (1.f + 0.5f * static_cast<float>(n & 1u)) * pow2f(static_cast<int>(two >> 1) - 1)
+                          : 0.5f * static_cast<float>(n & 1u);
+    const float s = __low2float(u32_as_h2(e4m3x2_to_h2(scales[row * (D / 16) + d / 16])));
+    return ((n & 8u) ? -mag : mag) * s;
+  }
+}
+
+// One row's result over keys [16 pg0, kend) of a range, key after key by a whole warp:
+// columns [col, col + D / 2), given the row's m and 1 / l (x 1 / gs_V).  For rows whose O a
+// NaN or an infinity spoiled that lies behind their last key (0 x NaN in the P V product),
+// which no pool of finite values brings here: it is out of line, and slow.
+template <int FMT, int D>
+__device__ __noinline__ void redo_row(const uint16_t* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                                      const uint8_t* v_codes, const uint8_t* v_scales, const int32_t* btab, int num_pages,
+                                      int num_kv_heads, int h, int pg0, int kend, int col, float scale, float m,
+                                      float inv, float* out) {
+  constexpr int EK = D / 32, EV = D / 64;  // elements of K and of V a lane
+  const int lane = threadIdx.x & 31;
+  float qv[EK], acc[EV];
+#pragma unroll
+  for (int e = 0; e < EK; ++e) qv[e] = __uint_as_float((uint32_t)q[EK * lane + e] << 16);
+#pragma unroll
+  for (int e = 0; e < EV; ++e) acc[e] = 0.f;
+  for (int key = pg0 * kPage; key < kend; ++key) {
+    const int id = btab[key / kPage];
+    if (id < 0 || id >= num_pages) continue;  // left out, as in the tiles
+    const int64_t row = ((int64_t)id * num_kv_heads + h) * kPage + key % kPage;
+    float z = 0.f;
+#pragma unroll
+    for (int e = 0; e < EK; ++e) z = fmaf(qv[e], pool_value<FMT, D>(k_codes, k_scales, row, EK * lane + e), z);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float pr = ex2(z * scale - m);
+#pragma unroll
+    for (int e = 0; e < EV; ++e) acc[e] = fmaf(pr, pool_value<FMT, D>(v_codes, v_scales, row, col + EV * lane + e), acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < EV; ++e) out[col + EV * lane + e] = acc[e] * inv;
+}
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPxSoft) : "memory"); }
 
 template <int FMT, int D, bool PLO>
@@ -962,13 +1012,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     // l = 0: no visible token (or only logits of -inf).  A NaN logit among the visible
     // ones makes l, and so the row's partial, NaN
     const bool any = ok && nt > 0 && l != 0.f;
-    float inv = any ? p.v_gs_inv / l : 0.f, unit = 1.f;
+    const float inv_l = any ? p.v_gs_inv / l : 0.f;
+    float inv = inv_l, unit = 1.f;
     if constexpr (FMT == KVQ_FMT_INT8) {  // 2^E in two factors: E reaches beyond one's exponents
       const int e = e_run == kNoScale ? 0 : e_run;
       inv *= pow2f(e / 2);
       unit = pow2f(e - e / 2);
     }
     if (grp == 0 && qoff[rl] >= 0) p.lse_part[orow_at[rl]] = any ? (m_fin + log2f(l)) * kLn2 : -INFINITY;
+    // rows that end inside the range: a key behind their last one has weight 0, but 0 x NaN is
+    // NaN, so their O is looked at (odd stays 0 while all of it is finite)
+    const bool ends = any && kend < key_end && qoff[rl] >= 0;
+    const bool look = __any_sync(0xffffffffu, ends);
+    float odd = 0.f;
     // Each warp writes its 32 rows' half of the columns, 32 columns at a time, through a
     // patch of shared memory of its own: 128 contiguous bytes of four rows a store.
     uint8_t* patch = smem + Lo::kOAt + warp * Lo::kOPatch;
@@ -988,6 +1044,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tmem_ld_wait();
       }
       __syncwarp();  // the patch has been read
+      if (look) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(ov[e]), 0.f, odd);
+      }
 #pragma unroll
       for (int v4 = 0; v4 < 8; ++v4) {
         float4 o;
@@ -1003,6 +1063,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const float4 o = *reinterpret_cast<const float4*>(patch + (4 * x + sub) * Lo::kORow + 16 * c4);
         if (at[x] >= 0) *reinterpret_cast<float4*>(p.o_part + (size_t)at[x] * D + col + 4 * c4) = o;
       }
+    }
+    __syncwarp();  // a row that is made again is written after this
+    for (unsigned redo = __ballot_sync(0xffffffffu, ends && odd != 0.f); redo; redo &= redo - 1) {
+      const int src = __ffs(redo) - 1, r = 32 * w4 + src;
+      redo_row<FMT, D>(reinterpret_cast<const uint16_t*>(p.q) + (size_t)qoff[r] * D, p.k_codes, p.k_scales, p.v_codes,
+                       p.v_scales, btab, p.num_pages, p.num_kv_heads, h, pg0, __shfl_sync(0xffffffffu, kend, src),
+                       grp * (D / 2), p.sm_scale_log2 * p.k_gs_inv, __shfl_sync(0xffffffffu, m_fin, src),
+                       __shfl_sync(0xffffffffu, inv_l, src), p.o_part + (size_t)orow_at[r] * D);
     }
   }
   // all TMEM reads and MMAs are complete: free the columns

@@ -155,3 +155,48 @@ def test_scales_of_either_sign(out_dtype, which):
         dev.mul_(torch.from_numpy(sign).cuda())
     c.launch(checked=True)
     _check(c, 1.0, pools)
+
+
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("fmt", ["int8", "nvfp4", "bf16"])
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,splits,name", [(1, 1, "tiny_int8"), (3, 1, "serving_int8"), (3, 4, "tiny_int8")])
+def test_v_behind_a_rows_last_token_does_not_reach_it(T, splits, name, fmt, out_dtype, value):
+    """V of shared token 304 holds a NaN or an infinity.  Sequences of 700 and 710 tokens see it, one of 305 with its
+    last query token only, one of 290 and an empty one never: their rows are as without it, and of the rows that see it
+    the columns that it is in are not finite.  (Two results of one row differ by their roundings: the tolerance is
+    twice that of each.)"""
+    if fmt == "nvfp4" and value == "inf":
+        pytest.skip("E4M3 has no infinity")
+    wl = _share(W.make(name, lens=("list", [700, 710, 290, 305, 0]), seed=99), [0, 5], [640])
+    gs = H.global_scales(wl, fmt)
+    c = _Call(wl, fmt, [0, 5], [640], T=T, splits=splits, out_dtype=out_dtype, gs=gs)
+    c.launch(checked=True)
+    out, lse = c.out.clone(), c.lse.clone()
+    _, vc, _, vs = c.cache.views()
+    page, head, row = int(wl.block_tables[0, 304 // 16]), 1, 304 % 16
+    cols = slice(0, wl.D)
+    if fmt == "bf16":
+        vc[page, head, row].view(torch.bfloat16)[7] = float(value)
+        cols = slice(7, 8)
+    elif fmt == "int8":
+        vs[page, head, row] = float(value)
+    else:
+        vs[page, head, row, 3] = 0x7F
+        cols = slice(48, 64)
+    c.launch(checked=True)
+    G = wl.Hq // wl.Hkv
+    hit = torch.zeros(c.out.shape, dtype=torch.bool, device="cuda")
+    heads = slice(G * head, G * head + G)
+    hit[:2, :, heads, cols] = True
+    hit[3, T - 1, heads, cols] = True
+    assert not torch.any(torch.isfinite(c.out[hit]))
+    # INT8: the weights are formed as 2^(z - m + d), d the exponent of a half tile's V under the largest of the range (here
+    # that of the NaN or infinity: d = -60); a number below 2^7 is rounded by up to 2^-18, and so is the weight
+    fin = torch.isfinite(lse)
+    assert torch.equal(torch.isfinite(c.lse), fin) and (c.lse[fin] - lse[fin]).abs().max() <= 2.0 ** -17
+    others = torch.ones(wl.Hq, dtype=torch.bool)
+    others[heads] = False
+    assert torch.equal(c.out[:, :, others], out[:, :, others]) and torch.equal(c.lse[:, :, others], lse[:, :, others])
+    a, b = c.out[~hit].float(), out[~hit].float()
+    assert torch.all((a - b).abs() <= (4e-3 if out_dtype == "f32" else torch.clamp(2.0 ** -7 * b.abs(), min=2e-2)))
