@@ -83,17 +83,22 @@ class DecodePlan:
         return B.kvq_workspace_partials(self.workspace, self.total_splits, self.num_q_heads, self.head_dim)
 
 
-def _own_pages_only(plan):
+def _own_pages_only(plan, num_seqs=None):
     prefix = getattr(plan, "prefix", None)
     if prefix is not None and prefix.splits:
         raise ValueError("the plan leaves shared pages out: use prefix_decode")
+    made_for = getattr(plan, "num_seqs", num_seqs)  # a DevicePlan's
+    if num_seqs is not None and made_for != num_seqs:
+        raise ValueError(f"the plan is for {made_for} sequences, q has {num_seqs}")
 
 
 def decode(cache, plan, q, block_tables, seq_lens, out, sm_scale, lse_out=None, checked=False, skip_merge=False,
            early_start=False, stream=None):
     """early_start: the plan and block tables are not written by the kernel just before this call on the stream
     (e.g. they were uploaded once for all layers of a step), so the decode may read them early."""
-    _own_pages_only(plan)
+    _own_pages_only(plan, q.shape[0])
+    if getattr(plan, "num_seqs", 0) and plan.q_len != 1:
+        raise ValueError(f"the plan is for q_len {plan.q_len}: use verify")
     flags = ((B.KVQ_CHECKED if checked else 0) | (B.KVQ_SKIP_MERGE if skip_merge else 0)
              | (B.KVQ_EARLY_START if early_start else 0))
     B.kvq_paged_decode_attention(cache.struct, q, sm_scale, block_tables, seq_lens, plan.plan, plan.total_splits,
@@ -103,7 +108,7 @@ def decode(cache, plan, q, block_tables, seq_lens, out, sm_scale, lse_out=None, 
 def verify(cache, plan, q, block_tables, seq_lens, out, sm_scale, lse_out=None, checked=False, skip_merge=False,
            early_start=False, stream=None):
     """Causal attention for q.shape[1] query tokens a sequence; plan: DecodePlan(..., q_len=q.shape[1])."""
-    _own_pages_only(plan)
+    _own_pages_only(plan, q.shape[0])
     if plan.q_len != q.shape[1]:
         raise ValueError(f"the plan is for q_len {plan.q_len}, q has {q.shape[1]} query tokens")
     flags = ((B.KVQ_CHECKED if checked else 0) | (B.KVQ_SKIP_MERGE if skip_merge else 0)

@@ -420,3 +420,34 @@ def test_default_key_ranges_stay_short_enough_for_fp32(kvq):
                 S = f(s, B, q, hq, 1, n, 152)
                 assert S == 0 or -(-n // 16) <= 256 * S, (fmt, B, q, n, S)
             assert f(s, B, q, hq, 1, 300000, 152) == 64
+
+
+def test_a_device_plan_is_for_its_own_batch(kvq, monkeypatch):
+    """decode and verify on a DevicePlan of another batch or query length: refused (on the GPU the plan's own check may
+    take an offset for its CTA count)."""
+    import torch
+
+    from quantized_paged_kv_gb300 import cache as C
+
+    calls = []
+    for name in ("kvq_paged_decode_attention", "kvq_paged_verify_attention"):
+        monkeypatch.setattr(kvq._binding, name, lambda *a: calls.append(a))
+
+    class Plan:
+        prefix, plan, total_splits, num_ctas, workspace = None, None, 0, 0, None
+
+        def __init__(self, q_len, num_seqs):
+            self.q_len, self.num_seqs = q_len, num_seqs
+
+    cache = type("Cache", (), {"struct": None})
+    one, three = torch.zeros(4, 8, 128), torch.zeros(4, 3, 8, 128)
+    C.decode(cache, Plan(1, 4), one, None, None, None, 1.0)
+    C.verify(cache, Plan(3, 4), three, None, None, None, 1.0)
+    assert len(calls) == 2
+    for plan in (Plan(1, 5), Plan(3, 4)):
+        with pytest.raises(ValueError):
+            C.decode(cache, plan, one, None, None, None, 1.0)
+    for plan in (Plan(3, 5), Plan(1, 4)):
+        with pytest.raises(ValueError):
+            C.verify(cache, plan, three, None, None, None, 1.0)
+    assert len(calls) == 2
