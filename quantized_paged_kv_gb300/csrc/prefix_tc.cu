@@ -1021,8 +1021,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     if (grp == 0 && qoff[rl] >= 0) p.lse_part[orow_at[rl]] = any ? (m_fin + log2f(l)) * kLn2 : -INFINITY;
     // rows that end inside the range: a key behind their last one has weight 0, but 0 x NaN is
-    // NaN, so their O is looked at (odd stays 0 while all of it is finite)
-    const bool ends = any && kend < key_end && qoff[rl] >= 0;
+    // NaN, so their O is looked at (odd stays 0 while all of it is finite).  A row whose l is
+    // NaN is NaN anyway
+    const bool ends = any && l == l && kend < key_end && qoff[rl] >= 0;
     const bool look = __any_sync(0xffffffffu, ends);
     float odd = 0.f;
     // Each warp writes its 32 rows' half of the columns, 32 columns at a time, through a

@@ -36,3 +36,15 @@ def test_head_counts(shape, T, out_dtype, fmt):
     border = 128 // (G * T)
     c.check(units=[(b, i, h) for b in {0, 1, border - 1, border, border + 1, n - 1, n, n + 2, n + 3} for i in range(T)
                    for h in sorted({0, Hkv // 2, Hkv - 1})])
+
+
+def test_the_largest_launch():
+    """4,096 launch sequences, the most that a device plan takes, in 500 groups and 24 lone sequences."""
+    lens = [17 + b % 40 for b in range(1024)]
+    offsets = [2 * g for g in range(501)]
+    wl = _share(W.make("serving_int8", lens=("list", lens), seed=104), offsets, [16] * 500)
+    wl = dataclasses.replace(wl, Hkv=1, Hq=3)
+    c = _Call(wl, "int8", offsets, [16] * 500, T=4, splits=1)
+    assert c.plan.batch == 4096
+    c.launch(checked=True)
+    c.check(units=[(b, i, 0) for b in (0, 1, 2, 511, 998, 999, 1000, 1001, 1023) for i in (0, 3)])

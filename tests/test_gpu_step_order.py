@@ -77,3 +77,36 @@ def test_nothing_shared_without_groups():
                                  plan.workspace, out, lse, B.KVQ_CHECKED)
     assert (out - want).abs().max() <= 4e-3  # each within 2e-3 of the oracle
     assert torch.equal(torch.isneginf(lse), (sl == 0)[:, None].expand_as(lse))
+
+
+def test_two_steps_at_once():
+    """Two streams, each with its own tables, plan and workspaces, over one pool: the same bits as one after the other."""
+    from quantized_paged_kv_gb300 import StepTables, build_tables
+
+    calls, tables, want = [], [], []
+    for k, (fmt, T, out_dtype) in enumerate((("int8", 1, "f32"), ("int8", 3, "bf16"))):
+        wl = _share(W.make("tiny_int8", lens=("list", [1200, 900, 1000, 40, 1300]), seed=110), [0, 5], [640])
+        c = _Call(wl, fmt, [0, 5], [640], T=T, splits=3, out_dtype=out_dtype)
+        c.cache = calls[0].cache if calls else c.cache
+        c.launch(checked=True)
+        calls.append(c)
+        want.append((c.out.clone(), c.lse.clone()))
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        t = StepTables(torch.full((300, 40), -1, dtype=torch.int32, device="cuda"), 300 * 200)
+        args = i32([3 * k] * 300), i32([100 + (7 * b + k) % 300 for b in range(300)]), i32(list(range(k, 6000 + k)))
+        cache = type("Pool", (), {"struct": c.cache.struct})
+        build_tables(cache, t, *args, i32([0]))
+        tables.append((t, args, t.slot_mapping.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(50):
+        for c, (t, args, _), s in zip(calls, tables, streams):
+            with torch.cuda.stream(s):
+                c.out.fill_(float("nan"))
+                t.slot_mapping.fill_(-7)
+                t.free_head.zero_()
+                build_tables(type("Pool", (), {"struct": c.cache.struct}), t, *args)
+                c.launch()
+    torch.cuda.synchronize()
+    for c, (t, _, slots), (out, lse) in zip(calls, tables, want):
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse) and torch.equal(t.slot_mapping, slots)
