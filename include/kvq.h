@@ -461,6 +461,7 @@ int kvq_paged_prefill_attention(const kvq_cache* cache, const void* q, int32_t q
  *   flags          KVQ_CHECKED: synchronize and read the status word
  * seq_lens may be ctx_lens and free_head_out may be free_head (a captured step then
  * advances its own state); no other output may overlap an input.
+ * A head outside the list is flagged (KVQ_DEV_NO_PAGE) and taken as its nearer end.
  * A request with a negative length, or one that would not fit its table row, adds
  * nothing (seq_lens = its ctx clamped to the row; KVQ_DEV_BAD_SEQLEN).  Where the
  * free list ends the entries are -1 (KVQ_DEV_NO_PAGE).  A token whose page id is
@@ -501,8 +502,12 @@ typedef struct kvq_prefix {
  * take about 1.1 us instead of its 1.9), for prefix_len shared tokens (the longest
  * group's) and num_groups groups, among those whose key ranges hold at most 4,096 tokens
  * (64 where that takes more: past 262,144 shared tokens); 0 where the sequences
- * are expected to read the shared pages faster each for itself (few sequences or a
- * short prefix: under about 45,000 shared tokens x sequences at 4 KV heads of 256).
+ * are expected to read the shared pages faster each for itself: few sequences or a
+ * short prefix.  With one query token, 6 query heads a KV head and 152 SMs that is under
+ * about 50,000 shared tokens x sequences from 8 sequences on at 4 KV heads of 256 (65,000
+ * at 4 sequences, 87,000 at 3, never at 2), under about 27,000 at 8 heads of 128.  Every
+ * sequence counts as sharing prefix_len tokens: with short groups or lone sequences
+ * among them sharing is taken to pay more than it does.
  * >= 0, or minus a kvq_status.  target_ctas: the SM count (0: the current device's). */
 int32_t kvq_prefix_splits(const kvq_cache* cache, int32_t batch, int32_t q_len, int32_t num_q_heads,
                           int32_t num_groups, int32_t prefix_len, int32_t target_ctas);
@@ -560,7 +565,8 @@ int kvq_plan_splits_device(const kvq_cache* cache, const int32_t* seq_lens, int3
  *   plan           device, kvq_plan_splits_device with the same lengths and prefix;
  *                  total_splits and num_ctas as given there
  *   workspace      device, >= kvq_decode_workspace_bytes(total_splits, num_q_heads, head_dim),
- *                  256-byte aligned, its status block zero before the first call; with
+ *                  256-byte aligned, its status block zero before the first call, another one
+ *                  (and another plan) for a call that may run at the same time; with
  *                  kvq_verify_workspace_bytes a call of several query tokens that shares
  *                  nothing (splits = 0) may take the verify call's tensor-core route
  *   out, lse_out   device, as for the decode (lse_out nullable)
