@@ -33,6 +33,10 @@
 //     memory by cp.async, unconverted.
 // The code is kept short (loops where registers allow): the roles run different code at
 // once, and instruction fetch was a third of the warps' stalls.
+// Measured (the kernel alone, nothing in L2): INT8, 4 heads of 256, fp32 output, 192 rows a
+// head on 32K tokens 46.6 us, 553 TFLOP/s of q K and P V and 1,106 with P's lo terms and the
+// empty rows of the second block (measured bf16 rate 1,951); INT8, 8 heads of 128, bf16 output,
+// 256 rows a head on 2,048 tokens 11.7 us, 184 TFLOP/s: mostly a CTA's start and end.
 // Every wait is bounded (%globaltimer); a timeout sets KVQ_DEV_TIMEOUT, the CTA waits
 // for its issued MMAs, frees its TMEM and returns.
 #include "tc_tile.cuh"
