@@ -1125,11 +1125,11 @@ int32_t kvq_prefix_splits(const kvq_cache* cache, int32_t batch, int32_t q_len, 
   // verify call's tensor-core route for them; fitted at 1 .. 64 sequences and 1 or 4 query
   // tokens on 256 .. 32K shared tokens, all formats (597 calls): the choice loses 0.08 us
   // in the mean, at most 12 % (33 % for 64 x 4 tokens on 256, NVFP4).  us shared / alone,
-  // INT8, 4 KV heads of 256, 6 query heads each, fp32 out (64 on 512 is a case where the
-  // model takes the slower side: 15.1 against 10.9, so it does not share):
-  //   4 sequences:  512 tokens 19.7 / 11.0, 8K 26.3 / 19.7, 32K 42.3 / 48.6
-  //   16 sequences: 512 21.9 / 13.4, 2K 23.8 / 20.6, 4K 25.7 / 30.7, 32K 47.8 / 166
-  //   64 sequences: 256 22.9 / 19.7, 512 23.9 / 25.2, 16K 52.9 / 359
+  // INT8, 4 KV heads of 256, 6 query heads each, fp32 out, own parts up to 64 tokens:
+  //   4 sequences:  512 tokens 21.0 / 10.4, 8K 24.6 / 19.1, 32K 38.1 / 47.5
+  //   16 sequences: 512 20.8 / 11.8, 2K 21.5 / 19.6, 4K 23.8 / 29.4, 32K 41.4 / 166
+  //   64 sequences: 256 21.5 / 15.2, 512 22.4 / 20.8 (longer own parts, an earlier build: 23.9 /
+  //   25.2, where the rule, which does not share, takes the slower side), 16K 46.4 / 361
   const int64_t waves = (items * S + sms - 1) / sms, tiles = (pages + 4 * S - 1) / (4 * S);
   const double width = cache->head_dim / 256.0;
   const double shared_us =
