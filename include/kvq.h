@@ -571,6 +571,8 @@ int kvq_plan_splits_device(const kvq_cache* cache, const int32_t* seq_lens, int3
  *                  nothing (splits = 0) may take the verify call's tensor-core route
  *   out, lse_out   device, as for the decode (lse_out nullable)
  *   flags          KVQ_CHECKED: synchronize and read the status word
+ * On a BF16 cache the weights go to the tensor cores as two bf16 terms whatever the output's
+ * type (the decode and verify calls take one for bf16 output).
  * A row that sees no token gives out = 0, lse = -inf.  A plan made for other
  * lengths, groups or splits gives wrong results within bounds; where a sequence has
  * too few partial slots it sets KVQ_DEV_BAD_PLAN.

@@ -674,7 +674,7 @@ namespace {
 int prefill_launch(const kvq_cache* cache, const void* q, int32_t batch, int32_t q_len, int32_t num_q_heads,
                    float sm_scale, const int32_t* block_table, int32_t max_pages, int32_t seq_len,
                    const int32_t* seq_len_dev, int32_t splits, void* workspace, void* out, int32_t out_dtype,
-                   float* lse_out, uint32_t flags, void* stream) {
+                   float* lse_out, uint32_t flags, void* stream, bool two_terms = false) {
   const int D = cache->head_dim;
   const int G = num_q_heads / cache->num_kv_heads;
   kvq::PrefillInstance inst;
@@ -729,6 +729,7 @@ int prefill_launch(const kvq_cache* cache, const void* q, int32_t batch, int32_t
   p.splits = splits;
   p.row_blocks = (q_len * G + inst.rows - 1) / inst.rows;
   p.out_bf16 = out_dtype == KVQ_OUT_BF16;
+  p.two_terms = two_terms ? 1 : 0;
   p.sm_scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   p.k_gs_inv = cache->format == KVQ_FMT_NVFP4 ? 1.0f / cache->k_global_scale : 1.0f;
   p.v_gs_inv = cache->format == KVQ_FMT_NVFP4 ? 1.0f / cache->v_global_scale : 1.0f;
@@ -1271,7 +1272,7 @@ int kvq_paged_prefix_attention(const kvq_cache* cache, const void* q, int32_t ba
     const int S = verify_route_splits(cache, batch, q_len, num_q_heads, max_pages_per_seq, 0);
     if (S > 0 && workspace_bytes >= kvq_prefill_workspace_bytes(batch * q_len, num_q_heads, D, S))
       return prefill_launch(cache, q, batch, q_len, num_q_heads, sm_scale, block_tables, max_pages_per_seq, 0, seq_lens,
-                            S, workspace, out, out_dtype, lse_out, flags, stream);
+                            S, workspace, out, out_dtype, lse_out, flags, stream, cache->format == KVQ_FMT_BF16);
   }
   // row blocks: rows / 128 rounded up in every group
   const int64_t rows = V * G;
@@ -1330,6 +1331,7 @@ int kvq_paged_prefix_attention(const kvq_cache* cache, const void* q, int32_t ba
   p.total_splits = total_splits;
   p.item_splits = static_cast<int32_t>(T);
   p.out_bf16 = x.out_bf16;
+  p.two_terms = cache->format == KVQ_FMT_BF16;  // as the prefix kernel
   p.wait_limit_ns = 2000000000ull;  // 2 s
   p.early_start = prefix->splits > 0 ? 2 : 0;  // 2: beside the prefix kernel, whose preceding kernels are done
   p.q_len = q_len;

@@ -33,9 +33,10 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // fp32 output: P' = hi + lo terms; bf16 output: the hi term alone
-  return p.out_bf16 ? cudaLaunchKernelEx(&cfg, decode_kernel<FMT, D, false>, tk, tv, p)
-                    : cudaLaunchKernelEx(&cfg, decode_kernel<FMT, D, true>, tk, tv, p);
+  // fp32 output: P' = hi + lo terms; bf16 output: the hi term alone unless the call wants both
+  return p.out_bf16 && !p.two_terms
+             ? cudaLaunchKernelEx(&cfg, decode_kernel<FMT, D, false>, tk, tv, p)
+             : cudaLaunchKernelEx(&cfg, decode_kernel<FMT, D, true>, tk, tv, p);
 }
 
 }  // namespace

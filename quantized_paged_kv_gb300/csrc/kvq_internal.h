@@ -28,6 +28,7 @@ struct DecodeParams {
   int32_t q_len;               // query tokens a sequence: batch = sequences x q_len virtual sequences
   int32_t heads_per_cta;       // KV heads per work item (a divisor of num_kv_heads)
   int32_t out_bf16;
+  int32_t two_terms;           // P' = hi + lo with bf16 output too
   int32_t early_start;         // 1: read plan / block tables before waiting for the preceding kernel;
                                // 2: behind the prefix kernel, wait for it at the end only
   int32_t out_host;            // out is pinned host memory: direct rows are written with plain stores
@@ -52,6 +53,7 @@ struct PrefillParams {
   const int32_t* seq_len_dev;  // device [batch]: the sequence lengths, read by the kernel (null: seq_len, batch 1)
   int32_t batch, q_len, seq_len, num_q_heads, num_kv_heads, num_pages, max_pages;
   int32_t splits, row_blocks, out_bf16;
+  int32_t two_terms;           // P' = hi + lo with bf16 output too
   float sm_scale_log2;
   float k_gs_inv, v_gs_inv;    // NVFP4: 1 / global scales (1 otherwise)
 };
@@ -146,7 +148,7 @@ struct PrefillInstance {
 
 // the shared-prefix kernel (prefix_tc.cu)
 struct PrefixInstance {
-  const void* kernels[2];      // [0] fp32 output (P' hi + lo), [1] bf16 output (hi)
+  const void* kernels[2];      // [0] fp32 output (P' hi + lo), [1] bf16 output (hi; BF16 cache: the same as [0])
   int smem_bytes;
   int threads;
   int rows;                    // query rows of a work item

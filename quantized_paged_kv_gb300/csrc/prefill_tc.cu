@@ -640,8 +640,8 @@ cudaError_t launch_tc_t(const PrefillParams& p, int grid, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.out_bf16 ? cudaLaunchKernelEx(&cfg, prefill_tc_kernel<FMT, D, false>, p)
-                    : cudaLaunchKernelEx(&cfg, prefill_tc_kernel<FMT, D, true>, p);
+  return p.out_bf16 && !p.two_terms ? cudaLaunchKernelEx(&cfg, prefill_tc_kernel<FMT, D, false>, p)
+                                    : cudaLaunchKernelEx(&cfg, prefill_tc_kernel<FMT, D, true>, p);
 }
 
 template <int FMT, int D>

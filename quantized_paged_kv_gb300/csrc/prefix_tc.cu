@@ -20,7 +20,7 @@
 //     tile's exponentials run while the tensor cores and the other group work on its
 //     neighbours.  One row a thread: S from TMEM, the online softmax, P over S(i) in
 //     TMEM as the A operand of the P V product (hi + lo terms when the call's output
-//     is fp32).  The groups share the rows' running references (they scale one O): the
+//     is fp32, or the cache BF16).  The groups share the rows' running references (they scale one O): the
 //     reference after tile i goes from warp to warp through shared memory, each row's
 //     sum stays with its group (two partial sums, joined at the end).
 //   * warp 8 (MMA): S(i) = Q K(i)^T into one of three (D = 128: four) TMEM
@@ -259,9 +259,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   // scale below 2^-14 of their largest is subnormal in fp16, its key's V off by up to 2^-24 of
   // the largest |V| among them, as P' is with the scales folded into it (see the softmax).
   // With fp32 output the tile holds the exact codes and the scales are folded into P.
-  // BF16 cache with bf16 output: P is one bf16 term, as in the decode kernel: up to 2^-8 a
-  // weight, like the output's own rounding (rms error 2.2e-3 in all where the output's
-  // rounding alone makes 1.7e-3).
   constexpr bool kFoldV = FMT == KVQ_FMT_INT8 && !PLO;
   constexpr uint32_t kIdescS = umma_idesc_f16(kPxRows, kPxKeys, kBf16, false);
   constexpr uint32_t kIdescPV = umma_idesc_f16(kPxRows, D, kBf16, true);
@@ -1087,6 +1084,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   }
 }
 
+// P as hi + lo terms: with fp32 output, and on a BF16 cache always (one bf16 term is off by up
+// to 2^-8 a weight, as much as bf16 output by its own rounding: rms 2.3e-3 in all against 1.7e-3;
+// the lo terms here and on the own pages cost 1.3 of 38.6 us with 45 sequences in three groups
+// on up to 4,096 tokens)
+template <int FMT>
+constexpr bool two_terms(bool out_f32) {
+  return out_f32 || FMT == KVQ_FMT_BF16;
+}
+
 template <int FMT, int D>
 cudaError_t launch_px_t(const PrefixParams& p, int blocks, cudaStream_t stream) {
   using Lo = PxLayout<FMT, D>;
@@ -1100,7 +1106,7 @@ cudaError_t launch_px_t(const PrefixParams& p, int blocks, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.out_bf16 ? cudaLaunchKernelEx(&cfg, prefix_tc_kernel<FMT, D, false>, p)
+  return p.out_bf16 ? cudaLaunchKernelEx(&cfg, prefix_tc_kernel<FMT, D, two_terms<FMT>(false)>, p)
                     : cudaLaunchKernelEx(&cfg, prefix_tc_kernel<FMT, D, true>, p);
 }
 
@@ -1108,7 +1114,7 @@ template <int FMT, int D>
 PrefixInstance px_instance_of() {
   using Lo = PxLayout<FMT, D>;
   return PrefixInstance{{reinterpret_cast<const void*>(&prefix_tc_kernel<FMT, D, true>),
-                         reinterpret_cast<const void*>(&prefix_tc_kernel<FMT, D, false>)},
+                         reinterpret_cast<const void*>(&prefix_tc_kernel<FMT, D, two_terms<FMT>(false)>)},
                         Lo::kSmemBytes,
                         kPxThreads,
                         kPxRows};

@@ -77,3 +77,24 @@ def test_int8_v_of_two_sizes_in_every_tile(ratio, out_dtype):
             bound = rel + 2e-5 * size + 2.0 ** -23 * vmax + lost
             d = np.abs(out[b, G * h:G * h + G] - ref)
             assert np.all(d <= bound), (d / bound).max()
+
+
+@pytest.mark.parametrize("T,splits,own", [(1, 2, 120), (1, 1, 0), (1, 0, 120), (6, 0, 120), (3, 2, 120)])
+@pytest.mark.parametrize("name", ["tiny_int8", "serving_int8"])
+def test_bf16_output_of_a_bf16_cache_is_the_rounded_result(T, splits, own, name):
+    """Shared and own pages, nothing shared (T = 6: the tensor-core route of several query tokens): the output is within
+    half a bf16 step of the result and what fp32 output is off by: n / 8 x 2^-23 (at most one unit a product) and 2^-17
+    of sum w |v|.  One bf16 term of P would add up to 2^-9 (half a step of a number in [1, 2), relative to 1) a weight."""
+    n = 704
+    wl = _one_group(name, [n + own, n + own // 2, n], n, 105)
+    c = _Call(wl, "bf16", [0, 3], [n], T=T, splits=splits, out_dtype="bf16")
+    c.launch(checked=True)
+    pools = H.oracle_pools(wl, "bf16")
+    flat = dict(pools, v_codes=(pools["v_codes"].view(np.uint16) & 0x7FFF).view(np.uint8))
+    verify = lambda p: oatt.paged_verify("bf16", p, c.q, wl.block_tables, wl.seq_lens, wl.sm_scale)[0]
+    ref, size = verify(pools), verify(flat)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 7)
+    # a result just below a power of two may be rounded in the upper binade's steps
+    bound = step / 2 * 2.0 ** (np.abs(ref) > 0.999 * 2 ** 8 * step) + ((n + own) / 8 * 2.0 ** -23 + 2.0 ** -17) * size
+    d = np.abs(c.out.float().cpu().numpy() - ref)
+    assert np.all(d <= bound), (d / bound).max()
