@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   constexpr uint32_t kIdescS = umma_idesc_f16(kPxRows, kPxKeys, kBf16, false);
   constexpr uint32_t kIdescPV = umma_idesc_f16(kPxRows, D, kBf16, true);
   static_assert(kBarCount <= Lo::kNumBars, "barriers");
+  static_assert(PLO || !kBf16, "a BF16 cache always takes two terms");
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -948,12 +949,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             pv = mul2(pv, (x & 1) ? pair(v4.z, v4.w) : pair(v4.x, v4.y));
           const float2 v = unpair(pv);
           if constexpr (!PLO) {
-            if constexpr (kBf16) {
-              const __nv_bfloat162 hv = __floats2bfloat162_rn(v.x, v.y);
-              ph[x] = *reinterpret_cast<const uint32_t*>(&hv);
-            } else {
-              ph[x] = h2_as_u32(__floats2half2_rn(v.x, v.y));
-            }
+            ph[x] = h2_as_u32(__floats2half2_rn(v.x, v.y));
           } else {
             // hi + lo, lo = what hi leaves of p', rounded: fp16 hi cut off to 11 bits (22 kept
             // in all), bf16 hi rounded to 8 (the rest is then half as large, and both
